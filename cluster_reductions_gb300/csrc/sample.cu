@@ -682,6 +682,13 @@ __device__ __forceinline__ void add_dsmem_u32(uint32_t addr, uint32_t n) {
 // at the kernel's end; sorting and narrowing it does alone.  True when that
 // last meeting is behind this CTA.
 // (MANY: C > 1.)
+//
+// What holds between the stages: every count that a cut is taken from (bins,
+// lists) is one of tokens with weight, x >= low, so a list has the entry that
+// its bin's count promises, and a count below top_k means that top-k keeps
+// all that has weight.  `cut` keeps wholly what lies above its key and the
+// first `ties` of what is at it; seg holds a segment's mass above the key (of
+// what min_p leaves) and tie the number of its tokens at the key.
 enum Order : uint32_t { kNothing, kCount, kGather };
 
 template <class E, int T, int kSub, bool MANY>
@@ -790,6 +797,7 @@ __device__ __forceinline__ bool sample_row(const SampleArgs &a, unsigned char *s
     if (keyed) {
       // (sh.cnt was cleared at the start)
       uint64_t near = 0;
+      uint32_t bare = 0;   // near ones without weight, which bin P must not count
       row.template each<T>(s0, s1, [&](int un, uint4 (&v)[kSub]) {
         row.parts(un, v, [&](int, const uint4 &q) {
           uint32_t least = ~0u;
@@ -805,13 +813,19 @@ __device__ __forceinline__ bool sample_row(const SampleArgs &a, unsigned char *s
 #pragma unroll 1
             for (int j = 0; j < N; ++j) {
               const float x = element_of(q, j);
-              if (kb.is_near(x) && x >= rs.low) near += rs.weight(x, sh.tab);
+              if (!kb.is_near(x)) continue;
+              if (x >= rs.low) near += rs.weight(x, sh.tab);
+              else ++bare;
             }
           }
         });
       });
       near = warp_sum(near);
-      if (lane == 0) sh.wc[w] = near;
+      bare = __reduce_add_sync(0xffffffffu, bare);
+      if (lane == 0) {
+        sh.wc[w] = near;
+        if (bare) atomicSub(&sh.cnt[kb.P], bare);   // (modulo 2^32: in any order with the others' counts)
+      }
       if (tid == 0) sh.found = sh.found2 = -1;
       __syncthreads();
       uint64_t nears = warp_sum(lane < W ? sh.wc[lane] : 0), total;
@@ -838,7 +852,7 @@ __device__ __forceinline__ bool sample_row(const SampleArgs &a, unsigned char *s
             const uint64_t y = rs.weight(v, sh.tab);   // (anything where the bin has no value)
             const uint64_t x = b < kb.NB && b != kb.P && n && v >= rs.low ? y : 0;
             sh.mass[b] = x;
-            c += n;
+            c += b == kb.P || x ? n : 0;   // tokens with weight
             ms += b == kb.P ? nears : x * n;
           }
           c = __reduce_add_sync(0xffffffffu, c);
@@ -867,7 +881,7 @@ __device__ __forceinline__ bool sample_row(const SampleArgs &a, unsigned char *s
 #pragma unroll 1
             for (int i = 0; i < BPER; ++i) {
               const int b = b0 + 32 * i;
-              const uint64_t nc = sh.cnt[b], x = sh.mass[b], nm = b == kb.P ? nears : x * nc;
+              const uint64_t x = sh.mass[b], nc = b == kb.P || x ? sh.cnt[b] : 0, nm = b == kb.P ? nears : x * nc;
               const uint64_t ic = pc + warp_scan(nc, lane), im = pm + warp_scan(nm, lane);
               const uint32_t over = __ballot_sync(0xffffffffu, (by_mass ? im : ic) >= want);
               if (over) {
@@ -1492,6 +1506,10 @@ __device__ __forceinline__ bool sample_row(const SampleArgs &a, unsigned char *s
   // the segment's elements, 32 units to a warp
   if (w < kSub) {
     const int hit = sh.found, un = hit * kSegUnits + 32 * w + lane;
+    if (hit < 0) {   // no mass: the maximum has some, so it cannot be; nothing is read there
+      if (tid == 0) answer(-1, __int_as_float(0x7fc00000));
+      return false;
+    }
     const uint64_t total = sh.wa[1], target = sh.wa[2];
     const uint32_t kept = tie[hit];
     float e[N];
