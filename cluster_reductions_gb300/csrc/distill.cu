@@ -101,9 +101,11 @@ template <class E> __device__ __forceinline__ void put(E *p, float v) {
 //
 // Arithmetic.  Pass 1 takes y = x c as fma(x, c, -M), M the rounded product of
 // the thread's largest x and c, so its rounding drops out of s and of every
-// term; one packed instruction a pair.  Where M is not finite (a row of
-// nothing but -inf or the type's lowest value, +inf) the row is folded again,
-// differences first, and pass 2 does the same.
+// term; one packed instruction a pair.  The rounding is at most 64 octaves
+// while |M| < 2^31, which a sum of 2^31 terms has room for.  M starts at -2^31,
+// so what lies below (masks) adds 0.  Where the row's M is not between
+// those (a row of nothing but mask, +inf) the row is folded again, differences
+// first, and pass 2 does the same.
 //
 // Every wait is bounded.  The pairs go to two places in turn: a CTA writes
 // place A again only after every peer's next pair has reached it in place B,
@@ -202,14 +204,16 @@ __device__ __forceinline__ void unit_pairs(const uint4 &w, uint64_t (&p)[8 / siz
   }
 }
 
-// A thread's pair in base 2: M = max x c, s in two halves.
+constexpr float kFar = 2147483648.0f;   // 2^31 octaves: see Arithmetic
+
+// A thread's pair in base 2: M = max(x c, -kFar), s in two halves.
 struct Fold2 {
-  float M;
-  uint64_t ref, s;   // (-M, -M), or zeros while M is -inf
+  float M = -kFar;
+  uint64_t ref = f2_pack(kFar, kFar), s = 0;   // ref: (-M, -M)
   __device__ __forceinline__ void raise(float vmax, float c) {
     const float v = vmax * c;
     if (v > M) {
-      const float f = ex2_approx(M - v);   // 0 from -inf
+      const float f = ex2_approx(M - v);
       s = f2_mul(s, f2_pack(f, f));
       M = v;
       ref = f2_pack(-v, -v);
@@ -489,7 +493,7 @@ k_distill_ring(DistillArgs a, RingShape g, int *err) {
         ms2_warp(m, s, 1.0f);
         wait(&tfull[h], turn(i));   // the logits at the entries have been read
         join_pairs(m, s, 1.0f);
-        const bool careful = !(fabsf(m) < INFINITY);
+        const bool careful = !(fabsf(m) < kFar);
         if (careful) {
           m = -INFINITY;
           s = 0.0f;
@@ -549,7 +553,7 @@ k_distill_ring(DistillArgs a, RingShape g, int *err) {
     auto pass1 = [&](int64_t item, int i) {
       const int h = i & 1;
       const Part<E> part(a, g, item, (int)r, false);
-      Fold2 fold{-INFINITY, 0, 0};
+      Fold2 fold;
       walk(part.nu, [&](int, int n, const uint4 *base) {
         uint4 w[kRingUnits];
 #pragma unroll
