@@ -106,6 +106,11 @@ template <class E> __device__ __forceinline__ void put(E *p, float v) {
 // so what lies below (masks) adds 0.  Where the row's M is not between
 // those (a row of nothing but mask, +inf) the row is folded again, differences
 // first, and pass 2 does the same.
+// kGrad's q = exp(x / T - lse) is off by the roundings of numbers of the lse's
+// size, up to six of them: 2^-13 of q at |lse| = 256, all of it at 10^7 (a row of
+// nothing but mask).  Past 256 the pair is taken from the row, by the consumers
+// of the CTA that has its first slice; it then writes the whole row and the
+// others nothing of it, since dx may be x.
 //
 // Every wait is bounded.  The pairs go to two places in turn: a CTA writes
 // place A again only after every peer's next pair has reached it in place B,
@@ -125,6 +130,29 @@ struct RingShape {
   int P;             // pieces of the ring
   int lg_tab;        // log2 of the places of the finisher warp's table
 };
+
+// A row by n threads, this one t: f(element, value) for the elements outside
+// its whole 16-byte units, g(first element, unit) for those, four at a time.
+template <class E, class F, class G>
+__device__ __forceinline__ void each_of_row(const E *x, int64_t V, int t, int n, F f, G g) {
+  constexpr int N = 16 / (int)sizeof(E);
+  const int64_t head = min(V, (int64_t)((-(uintptr_t)x & 15) / sizeof(E)));
+  const int64_t units = (V - head) / N, rest = V - head - units * N;
+  const uint4 *u = reinterpret_cast<const uint4 *>(x + head);
+  for (int64_t b = t; b < units; b += 4 * n) {
+    uint4 w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (b + k * n < units) w[k] = u[b + k * n];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (b + k * n < units) g(head + (b + k * n) * N, w[k]);
+  }
+  if (t < head + rest) {   // at most 2 N - 2 of them
+    const int64_t j = t < head ? t : units * N + t;
+    f(j, value(x + j));
+  }
+}
 
 // A CTA's part of an item.
 template <class E>
@@ -205,6 +233,10 @@ __device__ __forceinline__ void unit_pairs(const uint4 &w, uint64_t (&p)[8 / siz
 }
 
 constexpr float kFar = 2147483648.0f;   // 2^31 octaves: see Arithmetic
+// Whether q has to come from the row instead of its lse (NaN: the row's q are
+// NaN either way).
+__device__ __forceinline__ bool lse_coarse(float lse) { return fabsf(lse) > 256.0f; }
+enum { kSlice = 0, kWhole = 1, kNothing = 2 };   // kGrad: what of a row an item writes
 
 // A thread's pair in base 2: M = max(x c, -kFar), s in two halves.
 struct Fold2 {
@@ -306,7 +338,8 @@ k_distill_ring(DistillArgs a, RingShape g, int *err) {
   __shared__ __align__(8) float2 xpair[2][16];
   __shared__ float2 red[2][W];
   __shared__ struct { float m, s; int careful; } stat[2];          // the row's pair
-  __shared__ struct { float g, lse; int none; } given[2];          // grad_out, kGrad's lse, no gradient
+  // grad_out, kGrad's lse, no gradient, what is written
+  __shared__ struct { float g, lse; int none, what; } given[2];
   __shared__ int dead;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.K;
   const uint32_t C = cluster_nctarank(), r = cluster_ctarank();
@@ -360,8 +393,12 @@ k_distill_ring(DistillArgs a, RingShape g, int *err) {
     for (int64_t item = item0; item < g.items; item += step) {
       const Part<E> part(a, g, item, (int)r, MODE == kGrad);
       const E *x = reinterpret_cast<const E *>(a.x) + part.row * a.ldx;
-      if (MODE == kGrad && a.g[part.row] == 0.0f) {
-        // zeros: nothing is read
+      bool unread = false;
+      if constexpr (MODE == kGrad) {
+        const float gr = a.g[part.row], lse = a.lse[part.row];
+        unread = gr == 0.0f || lse_coarse(lse);
+      }
+      if (unread) {   // zeros, or what the consumers read themselves
         for (int k = 0; k < g.np; ++k, q.next(g.P), laps |= q.slot == 0) {
           wait(&empty[q.slot], q.phase ^ 1);
           if (lane == 0) mbar_arrive(&full[q.slot]);
@@ -411,7 +448,7 @@ k_distill_ring(DistillArgs a, RingShape g, int *err) {
     for (int64_t item = item0; item < g.items; item += step, ++i) {
       const int h = i & 1;
       const Part<E> part(a, g, item, (int)r, MODE == kGrad);
-      const int64_t b0 = max(part.first, (int64_t)0), b1 = min(part.first + (int64_t)part.nu * N, a.V);
+      int64_t b0 = max(part.first, (int64_t)0), b1 = min(part.first + (int64_t)part.nu * N, a.V);
       if (item + 2 * step < g.items) {   // the lists after the next: from DRAM by then
         const int64_t row = MODE == kGrad ? (item + 2 * step) / g.slices : item + 2 * step;
         const size_t ni = (size_t)K * (a.idx_wide ? 8 : 4), nt = (size_t)K * (a.t_bf16 ? 2 : 4);
@@ -422,7 +459,15 @@ k_distill_ring(DistillArgs a, RingShape g, int *err) {
       }
       float gr = 0.0f, lse = 0.0f;
       if constexpr (MODE != kLoss) gr = __ldg(a.g + part.row);
-      if constexpr (MODE == kGrad) lse = __ldg(a.lse + part.row);
+      int what = kSlice;
+      if constexpr (MODE == kGrad) {
+        lse = __ldg(a.lse + part.row);
+        if (lse_coarse(lse)) {
+          what = item % g.slices == 0 ? kWhole : kNothing;
+          b0 = 0;
+          b1 = what == kWhole ? a.V : 0;
+        }
+      }
       if (i >= 2) wait(&tfree[h], turn(i - 2));
       const bool any = teacher_warp<E>(a, part.row, lane, sidx + h * K, sp + h * K, slp + h * K,
                                        sx + h * K, MODE != kGrad && r == 0, b0, b1);
@@ -430,6 +475,7 @@ k_distill_ring(DistillArgs a, RingShape g, int *err) {
         given[h].g = gr;
         given[h].lse = lse;
         given[h].none = !any || (MODE != kLoss && gr == 0.0f);
+        given[h].what = what;
       }
       arrive(&tfull[h]);
     }
@@ -440,9 +486,14 @@ k_distill_ring(DistillArgs a, RingShape g, int *err) {
       for (int64_t item = item0; item < g.items; item += step, ++i) {
         const int h = i & 1;
         const Part<E> part(a, g, item, (int)r, MODE == kGrad);
-        const int64_t b0 = max(part.first, (int64_t)0), b1 = min(part.first + (int64_t)part.nu * N, a.V);
+        int64_t b0 = max(part.first, (int64_t)0), b1 = min(part.first + (int64_t)part.nu * N, a.V);
         wait(&tfull[h], turn(i));
         const bool on = !given[h].none;
+        const int what = MODE == kGrad ? given[h].what : kSlice;
+        if (what != kSlice) {
+          b0 = 0;
+          b1 = what == kWhole ? a.V : 0;
+        }
         if (on) merge_entries(sidx + h * K, sp + h * K, K, b0, b1, tkey, tsum, place, g.lg_tab, lane);
         wait(&done[h], turn(i));
         if (on) {
@@ -450,12 +501,13 @@ k_distill_ring(DistillArgs a, RingShape g, int *err) {
           const float gt = given[h].g * a.inv_T;
           E *dx = reinterpret_cast<E *>(a.dx) + part.row * a.lddx;
           float gq = 0.0f;
-          if constexpr (MODE == kBoth) gq = gt / stat[h].s;
+          if (MODE == kBoth || what == kWhole) gq = gt / stat[h].s;
           for (int k = lane; k < K; k += 32) {
             if (place[k] < 0) continue;
             const float v = sx[h * K + k], P = tsum[place[k]];
             float q;
-            if constexpr (MODE == kGrad) q = ex2_approx(fmaf(v, a.inv_T, -given[h].lse) * kLog2e) * gt;
+            if (MODE == kGrad && what == kSlice)
+              q = ex2_approx(fmaf(v, a.inv_T, -given[h].lse) * kLog2e) * gt;
             else q = (stat[h].careful ? ex2_approx((v - stat[h].m) * a.c)
                                       : ex2_approx(fmaf(v, a.c, -stat[h].m))) * gq;
             put(dx + sidx[h * K + k], q - gt * P);
@@ -615,6 +667,54 @@ k_distill_ring(DistillArgs a, RingShape g, int *err) {
         else
           return join<E, N>(e);
       };
+      const int what = MODE == kGrad && !none ? given[h].what : kSlice;
+      if (what != kSlice) {
+        walk(part.nu, [](int, int, const uint4 *) {});
+        if (what == kWhole) {
+          const E *x = reinterpret_cast<const E *>(a.x) + part.row * a.ldx;
+          float M = -INFINITY, s = 0.0f;
+          each_of_row(
+              x, a.V, tid, T,
+              [&](int64_t, float v) {
+                const float e[1] = {v};
+                ms2_fold<1>(M, s, e, a.c);
+              },
+              [&](int64_t, const uint4 &w) {
+                float e[N];
+                split<E, 16>(w, e);
+                ms2_fold<N>(M, s, e, a.c);
+              });
+          ms2_warp(M, s, a.c);
+          if (lane == 0) red[h][warp] = make_float2(M, s);
+          named_sync(1, T);   // and the row has been read
+          M = lane < W ? red[h][lane].x : -INFINITY;
+          s = lane < W ? red[h][lane].y : 0.0f;
+          ms2_warp(M, s, a.c);
+          if (tid == 0) {
+            stat[h].m = M;
+            stat[h].s = s;
+            stat[h].careful = 1;
+          }
+          const float f = gt / s;
+          each_of_row(
+              x, a.V, tid, T, [&](int64_t j, float v) { put(dx + j, ex2_approx((v - M) * a.c) * f); },
+              [&](int64_t j, const uint4 &w) {
+                float e[N];
+                split<E, 16>(w, e);
+#pragma unroll
+                for (int k = 0; k < N; ++k) e[k] = ex2_approx((e[k] - M) * a.c) * f;
+                if (same) {
+                  *reinterpret_cast<uint4 *>(dx + j) = join<E, N>(e);
+                } else {
+#pragma unroll
+                  for (int k = 0; k < N; ++k) put(dx + j + k, e[k]);
+                }
+              });
+          named_sync(1, T);   // red is free
+        }
+        arrive(&done[h]);
+        return;
+      }
       const bool plain = same && !none && !careful;
       walk(part.nu, [&](int pa, int n, const uint4 *base) {
         uint4 *dv = reinterpret_cast<uint4 *>(dx + part.first) + pa + tid;

@@ -655,7 +655,9 @@ int rr_distill_loss(const void *x, int64_t rows, int64_t V, int64_t ldx,
  * to x, given the lse of rr_distill_loss:
  *   dx_j = grad_out / T * (q_j - sum of p_k over the entries k that name j)
  * and 0 for rows without a valid entry or with grad_out = 0 (whose logits
- * are then not read).
+ * are then not read).  q = exp(x / T - lse) is right to about |lse| 2^-21 of
+ * itself; where |lse| > 256 (a row of nothing but a finite mask) it is taken
+ * from the row instead, and the lse only says so.
  *   dx       device, row i at dx + i * lddx elements, of x's dtype; x itself
  *            (with lddx = ldx) or memory that does not overlap x.
  *   lse, grad_out  device fp32 [rows].
