@@ -78,13 +78,17 @@ def _to_host(y: torch.Tensor, like: torch.Tensor) -> torch.Tensor:
 
 def _on_input_device(fn):
     """Run a binding call with the first argument's GPU as the current device
-    (the library launches on the current device and stream)."""
+    (the library launches on the current device and stream).  The argument
+    may come by its name."""
+    first = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(x, *args, **kwargs):
+    def call(*args, **kwargs):
+        x = args[0] if args else kwargs.get(first)
         if isinstance(x, torch.Tensor) and x.is_cuda and x.get_device() != torch.cuda.current_device():
             with torch.cuda.device(x.device):
-                return fn(x, *args, **kwargs)
-        return fn(x, *args, **kwargs)
+                return fn(*args, **kwargs)
+        return fn(*args, **kwargs)
     return call
 
 

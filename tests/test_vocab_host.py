@@ -119,3 +119,27 @@ def test_binding_refuses():
     for kind, call in calls:
         with pytest.raises(kind):
             call()
+
+
+def test_first_argument_by_name():
+    # every binding call takes its arguments by the names it documents: what
+    # follows are refusals of values, which a call that lost its first argument
+    # does not reach
+    import cluster_reductions_gb300 as rr
+    x, z = torch.zeros((3, 8)), torch.zeros(3, dtype=torch.int32)
+    calls = [
+        (ValueError, "weight must be", lambda: rr.embedding(weight=x[0], tokens=z)),
+        (ValueError, "dy must be", lambda: rr.embedding_grad(dy=x, tokens=z[:2], num_embeddings=5)),
+        (ValueError, "contiguous", lambda: rr.sample(x=x.t(), u=x[0])),
+        (ValueError, "contiguous", lambda: rr.distill_loss(x=x.t(), idx=z, teacher=z)),
+        (ValueError, "contiguous", lambda: rr.distill_grad(x=x.t(), idx=z, teacher=z, lse=z, grad_out=z)),
+        (ValueError, "contiguous", lambda: rr.distill_loss_grad(x=x.t(), idx=z, teacher=z, grad_out=z)),
+        (ValueError, "O must be", lambda: rr.splitk_combine(O=x, m=x, l=x, scale_log2e=1.0)),
+        (ValueError, "vals must be", lambda: rr.cluster_allreduce(vals=x)),
+        (ValueError, "contiguous", lambda: rr.softmax(x=x.t())),
+    ]
+    for kind, words, call in calls:
+        with pytest.raises(kind, match=words):
+            call()
+    with pytest.raises(TypeError, match="missing"):
+        rr.embedding(tokens=z)
