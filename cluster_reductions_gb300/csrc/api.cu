@@ -1005,6 +1005,7 @@ int rr_embedding_grad(const void *dy, int64_t n, int64_t D, int dtype, const voi
       overlaps(workspace, need, dw, ndw) || overlaps(workspace, need, dy, ndy) ||
       overlaps(workspace, need, tokens, ntok))
     return RR_ERR_INVALID;
+  if (!embedding_grad_fits(dy, n, D, dtype, dw, dw_dtype)) return RR_ERR_INVALID;
   int st = RR_OK;
   const DevInfo *d = current_device(&st);
   if (!d) return st;

@@ -493,6 +493,25 @@ int grad_chunk(int64_t n, int64_t D) {
   return L;
 }
 
+int64_t grad_tiles(int64_t D, int width) {
+  return (D + (int64_t)kGradThreads * width - 1) / ((int64_t)kGradThreads * width);
+}
+
+// Widest column group whose accesses of dy and dW are aligned (16 bytes at
+// most each; fp32 dW under bf16 dy takes two).
+int grad_column(const void *dy, int dtype, const void *dw, int dw_dtype, int64_t D) {
+  const int64_t es = dtype == RR_BF16 ? 2 : 4, gs = dw_dtype == RR_BF16 ? 2 : 4;
+  int width = dtype == RR_BF16 ? 8 : 4;
+  auto fits = [&](int64_t w) {
+    const int64_t gb = w * gs < 16 ? w * gs : 16;
+    const int64_t pb = w * 4 < 16 ? w * 4 : 16;   // the fp32 pieces
+    return D % w == 0 && (uintptr_t)dy % (w * es) == 0 && (D * es) % (w * es) == 0 &&
+           (uintptr_t)dw % gb == 0 && (D * gs) % gb == 0 && (D * 4) % pb == 0;
+  };
+  while (width > 1 && !fits(width)) width /= 2;
+  return width;
+}
+
 // The list of long runs: a count and a chunk each.
 size_t runs_bytes(int64_t chunks) { return ((size_t)(chunks + 1) * 4 + 255) & ~(size_t)255; }
 
@@ -503,9 +522,8 @@ int grad_launch(const void *dy, const int *key, const int *pos, int n, int64_t V
                 float scale, bool add, void *dw, float *piece, int *runs, cudaStream_t s,
                 const DevInfo &d) {
   const int L = grad_chunk(n, D);
-  const int64_t tiles = (D + (int64_t)kGradThreads * N - 1) / ((int64_t)kGradThreads * N);
-  const int64_t chunks = ((int64_t)n + L - 1) / L;
-  if (tiles * chunks > INT_MAX) return RR_ERR_INVALID;
+  const int64_t tiles = grad_tiles(D, N);
+  const int64_t chunks = ((int64_t)n + L - 1) / L;   // (embedding_grad_fits: tiles x chunks fit a grid)
   const dim3 grid((unsigned)(tiles * chunks)), block(kGradThreads);
   if (log_enabled())
     std::fprintf(stderr, "[rr] embedding gradient n=%d D=%lld chunk=%d width=%d grid=%u\n", n,
@@ -562,10 +580,16 @@ size_t embedding_grad_ws_bytes(int64_t n, int64_t D) {
   return 4 * list_bytes(n) + runs_bytes(chunks) + (chunks > 1 ? (size_t)chunks * 2 * D * sizeof(float) : 0);
 }
 
+bool embedding_grad_fits(const void *dy, int64_t n, int64_t D, int dtype, const void *dw, int dw_dtype) {
+  if (n == 0) return true;
+  const int L = grad_chunk(n, D);
+  return grad_tiles(D, grad_column(dy, dtype, dw, dw_dtype, D)) * ((n + L - 1) / L) <= INT_MAX;
+}
+
 int launch_embedding_grad(const void *dy, int64_t n, int64_t D, int dtype, const void *tok,
                           bool wide, int64_t V, float scale, void *dw, int dw_dtype, bool add,
                           void *ws, cudaStream_t s, const DevInfo &d) {
-  const int64_t es = dtype == RR_BF16 ? 2 : 4, gs = dw_dtype == RR_BF16 ? 2 : 4;
+  const int64_t gs = dw_dtype == RR_BF16 ? 2 : 4;
   SortArgs a;
   a.tok = tok;
   a.wide = wide;
@@ -626,16 +650,7 @@ int launch_embedding_grad(const void *dy, int64_t n, int64_t D, int dtype, const
   if (e != cudaSuccess || n == 0) return cuda_status(e);
   const int out = chip ? 0 : (a.passes - 1) & 1;
   const int *key = a.key[out], *pos = a.pos[out];
-  // widest column group whose accesses of dy and dW are aligned (16 bytes at
-  // most each; fp32 dW under bf16 dy takes two)
-  int width = dtype == RR_BF16 ? 8 : 4;
-  auto fits = [&](int64_t w) {
-    const int64_t gb = w * gs < 16 ? w * gs : 16;
-    const int64_t pb = w * 4 < 16 ? w * 4 : 16;   // the fp32 pieces
-    return D % w == 0 && (uintptr_t)dy % (w * es) == 0 && (D * es) % (w * es) == 0 &&
-           (uintptr_t)dw % gb == 0 && (D * gs) % gb == 0 && (D * 4) % pb == 0;
-  };
-  while (width > 1 && !fits(width)) width /= 2;
+  const int width = grad_column(dy, dtype, dw, dw_dtype, D);
   if (dtype == RR_F32)
     return grad_width<float, float>(width, dy, key, pos, a.n, V, D, scale, add, dw, piece, runs, s, d);
   if (dw_dtype == RR_F32)

@@ -238,6 +238,8 @@ int launch_embedding(const void *w, int64_t V, int64_t D, int dtype, const void 
 // Workspace of the gradient: the sorted list (two buffers of token and
 // position) and two fp32 rows of D per chunk of it.
 size_t embedding_grad_ws_bytes(int64_t n, int64_t D);
+// Whether the gradient's sums fit one grid (asked before the first launch).
+bool embedding_grad_fits(const void *dy, int64_t n, int64_t D, int dtype, const void *dw, int dw_dtype);
 // dw [V][D] of dw_dtype, added to when `add`, else written whole; ws
 // 16-byte aligned.  n at most 2^30, V at most 2^31 - 2.
 int launch_embedding_grad(const void *dy, int64_t n, int64_t D, int dtype, const void *tok,

@@ -53,6 +53,18 @@ def test_embedding_grad(lib):
         assert call(**bad) == INVALID, bad
 
 
+def test_embedding_grad_beyond_a_grid(lib):
+    # (chunks of the list) x (column tiles) past 2^31 - 1 is refused before the
+    # first launch, which would clear dw
+    n, D_ = 2**30, 2**24
+    need = ctypes.c_size_t()
+    assert lib.rr_embedding_grad_workspace_size(n, D_, ctypes.byref(need)) == OK
+    for add in (0, 1):
+        st = lib.rr_embedding_grad(1 << 60, n, D_, BF16, 1 << 57, I32, 10, f(1.0), 1 << 56, BF16, add, 1 << 58,
+                                   need.value, None)
+        assert st == INVALID
+
+
 def test_distill(lib):
     def loss(x=A, rows=3, V=100, ld=100, dt=BF16, idx=B, idt=I32, t=C, tdt=F32, K=5, T=1.0, lo=D, ls=E):
         return lib.rr_distill_loss(x, rows, V, ld, dt, idx, idt, t, tdt, K, f(T), lo, ls, None)
