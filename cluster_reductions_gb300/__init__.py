@@ -561,7 +561,9 @@ def embedding_grad(dy: torch.Tensor, tokens: torch.Tensor, num_embeddings: int,
     """rr_embedding_grad: the gradient of embedding() with respect to the
     [num_embeddings, D] table, from dy of the tokens' shape followed by D
     (bf16 or fp32).  Every row's terms are added in the tokens' order in
-    fp32 and rounded once to `dtype` (dy's dtype, the default, or float32).
+    fp32 (a token named more often than 16 to 256 times in pieces, joined in a
+    fixed order) and rounded once to `dtype` (dy's dtype, the default, or
+    float32).
     accumulate=True adds to `out` and touches only the rows that a token
     names.  The workspace (rr_embedding_grad_workspace_size bytes) is
     allocated here when not given."""
@@ -665,7 +667,8 @@ def distill_grad(x: torch.Tensor, idx: torch.Tensor, teacher: torch.Tensor, lse:
                  grad_out: torch.Tensor, temperature: float = 1.0, *,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """rr_distill_grad: the gradient of sum(grad_out * loss) with respect to x,
-    from distill_loss()'s lse; grad_out is fp32 [rows].  out may be x."""
+    from distill_loss()'s lse (rows whose |lse| is above 256 are summed anew);
+    grad_out is fp32 [rows].  out may be x."""
     dt = _float_dt(x, "x")
     xd, rows, V, ld = _rows_of(x, "x")
     gpu = xd.get_device()

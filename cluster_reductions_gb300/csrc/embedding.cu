@@ -7,8 +7,9 @@
 // A token outside [0, V) is padding: a row of zeros, and no part of the
 // gradient.  Both move bytes and compute next to nothing: DRAM bounds them.
 //
-// The gradient adds each table row's terms in increasing i, in fp32, with no
-// float atomics, so its bits do not depend on scheduling.  Three launches:
+// The gradient adds each table row's terms in increasing i, in fp32 (a long
+// run in pieces, the pieces joined in a fixed order), with no float atomics, so
+// its bits do not depend on scheduling.  Three launches:
 //
 //   k_token_sort   the first cluster sorts (token, i) stably by token: a
 //                  radix sort from the lowest digit, up to 9 bits a pass, the

@@ -10,9 +10,12 @@
 // A token is a whole number, so the answer has to be the one that exact
 // arithmetic gives.  fp32 sums over 10^5 weights are off by 1e-7 of the
 // total and would choose a neighbour in some per cent of the rows.  So the
-// weights are whole numbers of 2^-K (K about 62 - log2 V), right to about
-// 2^-31 of themselves, and every sum is a 64-bit integer sum: exact, and the
-// same however the row is split.
+// weights are whole numbers of 2^-K of the largest, K = 61 - ceil(log2 V), and
+// every sum is a 64-bit integer sum: exact, and the same however the row is
+// split.  A weight is right to about 2^-31 of itself and, cut to a whole number,
+// to 2^-K of the largest (44 bits at V = 131072, 41 at 2^20); together the cuts
+// are less than V 2^-K of the mass (2^-27 and 2^-21), by which the draw or the
+// end of top-p can differ from what exact weights would give.
 //
 // The weight.  With t = (x - max) * 256 log2(e) / T taken in two floats
 // (hi = the nearest whole number, g the rest), w = 2^(hi/256) * 2^(g/256):

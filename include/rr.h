@@ -693,8 +693,12 @@ int rr_distill_loss_grad(const void *x, int64_t rows, int64_t V, int64_t ldx,
  * exceeds u times the kept mass is drawn.  T <= 0 (or NaN) takes the first
  * largest logit.  Logits of -inf are never drawn; +inf ones share all mass.
  * A row with a NaN, or with nothing but -inf, gives token -1.
- * Masses are sums of whole numbers (w_j to about 2^-31 of itself), so the
- * token does not depend on how the row is split over the GPU.
+ * Masses are sums of whole numbers, so the token does not depend on how the
+ * row is split over the GPU: w_j is right to about 2^-31 of itself and to 2^-K
+ * (of the largest weight, 1), K = 61 - ceil(log2 V).  A row's mass is then
+ * off by less than V 2^-K of itself beside that (2^-27 at V = 131072, 2^-21 at
+ * 2^20); the token is the one of exact weights but where u times the kept mass,
+ * or the border of top_p, lies that close to another one's.
  *   x        device, row i at x + i * ldx elements, dtype RR_BF16 or RR_F32.
  *   u        device fp32 [rows], in [0, 1) (values outside are clamped).
  *   params   NULL (temperature 1, no filter), or the settings: scalars, and
