@@ -27,7 +27,7 @@
 // 36 K cycles that a row of 32003 bf16 alone on an SM takes under top-p, the
 // maximum is 3 K, counting the values 8 K, weighing 4096 bins and finding the
 // cut 9 K, the kept mass by segment 8 K, the draw 4 K.  Measured: 512 such rows
-// 48 us (676 GB/s), 256 x 131072 bf16 with mixed settings 65 us, 64 x 100003
+// 49 us (665 GB/s), 256 x 131072 bf16 with mixed settings 65 us, 64 x 100003
 // fp32 without filters 18.3 us, 1 x 131072 bf16 under top-k and top-p 15 us.
 #include <climits>
 #include <cstdio>

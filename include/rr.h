@@ -633,10 +633,13 @@ int rr_embedding_grad_workspace_size(int64_t n, int64_t D, size_t *bytes_out);
  *   loss  = sum_k p_k (log p_k - log q[idx_k])        (no factor T^2)
  * An entry whose t is -inf or whose idx lies outside [0, V) is not valid (a
  * shorter list, or a row without one: loss 0).  A vocabulary entry that is
- * named twice counts with both probabilities.  Terms with p_k = 0 count 0;
+ * named twice counts with both probabilities.  Terms with p_k = 0 in fp32
+ * (below 2^-126) count 0;
  * a valid entry with p_k > 0 on a student logit of -inf gives loss +inf.
  * Student logits of -inf have q = 0; a row of nothing else, or with a NaN or
- * +inf, gives NaN.
+ * +inf, gives NaN.  Finite masks of any size are numbers like others: a row of
+ * nothing but the type's lowest value is uniform (its lse is -inf where x / T
+ * is below the range of fp32).
  *   x        device, row i at x + i * ldx elements, dtype RR_BF16 or RR_F32;
  *            ldx >= V (rows >= 2); any element-aligned address.
  *   idx      device [rows][K] of idx_dtype RR_I32 or RR_I64.
